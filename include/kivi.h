@@ -442,7 +442,9 @@ int kivi_cache_copy(kivi_cache* dst, const kivi_cache* src, const int32_t* dst_s
  *   lambda = exp(lq1 . lk1) - exp(lq2 . lk2) + lambda_init,
  * and with a norm
  *   o = o * weight * (1 - lambda_init) / sqrt(mean(o^2) + norm_eps)
- * over a head's 2 d channels.  A sequence without tokens gives zeros. */
+ * over a head's 2 d channels.  A row that sees no token (a sequence without
+ * tokens, or a query whose window the cache no longer holds) gives zeros, also
+ * with norm_eps 0. */
 typedef struct kivi_diff_params {
   const float* lambdas;       /* device fp32 [4][d]: lq1, lk1, lq2, lk2; read by the launch */
   const float* norm_weight;   /* device fp32 [2 d], 8-byte aligned, or NULL: no norm (and no 1 - lambda_init) */

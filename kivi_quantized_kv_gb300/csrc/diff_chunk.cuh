@@ -888,7 +888,8 @@ __global__ void __launch_bounds__(512, AHEAD == 1 ? 2 : 1) diff_chunk_merge_kern
     ss = 0.f;
 #pragma unroll
     for (int w = 0; w < kWarps; ++w) ss += s_ss[w][lane];
-    const float f = rsqrtf(ss * (1.f / (2 * D)) + a.eps) * (1.f - a.lambda_init);
+    // a row of zeros (nothing seen, say) stays one, also where eps is 0
+    const float f = ss == 0.f ? 0.f : rsqrtf(ss * (1.f / (2 * D)) + a.eps) * (1.f - a.lambda_init);
 #pragma unroll
     for (int x = 0; x < C; ++x) o[x] *= f * __ldg(a.weight + warp * C + x);
   }

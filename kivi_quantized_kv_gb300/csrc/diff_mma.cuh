@@ -872,7 +872,8 @@ __global__ void __launch_bounds__(kDiffPairs * 64, 1) diff_mma_kernel(const __gr
       if (a.weight != nullptr) {
 #pragma unroll
         for (int x = 16; x > 0; x >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, x);
-        const float f = rsqrtf(ss * (1.f / (2 * D)) + a.eps) * (1.f - a.lambda_init);
+        // a row of zeros (nothing seen, say) stays one, also where eps is 0
+        const float f = ss == 0.f ? 0.f : rsqrtf(ss * (1.f / (2 * D)) + a.eps) * (1.f - a.lambda_init);
 #pragma unroll
         for (int i = 0; i < D / 32; ++i) {
           const float2 wt = __ldg(reinterpret_cast<const float2*>(a.weight) + lane + 32 * i);
