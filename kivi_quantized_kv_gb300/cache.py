@@ -80,11 +80,17 @@ class DiffWeights:
     """The learned weights of differential attention (include/kivi.h):
     lambdas [4, d] float32 (λq1, λk1, λq2, λk2), the layer's lambda_init, and
     the norm's weight [2 d] float32 with its eps, or None for no norm.  All on
-    the cache's device; the tensors are read by each launch (change them in
-    place, or make other DiffWeights)."""
+    the cache's device; each launch reads the tensors as they are then, changed
+    in place or with other storage (tensor.data = ...)."""
 
     def __init__(self, lambdas: torch.Tensor, lambda_init: float, norm_weight: torch.Tensor | None = None,
                  eps: float = 1e-5):
+        self._lambdas, self._norm_weight, self._lambda_init, self._eps = lambdas, norm_weight, lambda_init, eps
+        self._check()
+
+    def _check(self):
+        """Refuses tensors that a launch cannot read."""
+        lambdas, norm_weight = self._lambdas, self._norm_weight
         for t, what in ((lambdas, "lambdas"), (norm_weight, "norm_weight")):
             if t is None and what == "norm_weight":
                 continue
@@ -94,11 +100,21 @@ class DiffWeights:
             raise ValueError(f"lambdas must have shape (4, d), got {tuple(lambdas.shape)}")
         if norm_weight is not None and tuple(norm_weight.shape) != (2 * lambdas.shape[1],):
             raise ValueError(f"norm_weight must have shape {(2 * lambdas.shape[1],)}, got {tuple(norm_weight.shape)}")
-        self._lambdas, self._norm_weight, self._lambda_init, self._eps = lambdas, norm_weight, lambda_init, eps
-        self._c = _abi.KiviDiffParams(lambdas.data_ptr(), None if norm_weight is None else norm_weight.data_ptr(),
-                                      lambda_init, eps, 0)
 
-    # read-only: what a launch takes is laid out once, above
+    def _for(self, device: torch.device, d: int) -> _abi.KiviDiffParams:
+        """What a launch of a cache on `device` with this head_dim takes.  The
+        tensors are looked at in each call: their storage may have been exchanged."""
+        lam, norm = self._lambdas, self._norm_weight
+        f32 = torch.float32
+        if (lam.device != device or lam.shape != (4, d) or lam.dtype is not f32 or not lam.is_contiguous() or
+                (norm is not None and (norm.device != device or norm.shape != (2 * d,) or norm.dtype is not f32 or
+                                       not norm.is_contiguous()))):
+            self._check()
+            raise ValueError(f"the weights must be on {device} and of head_dim {d}")
+        return _abi.KiviDiffParams(lam.data_ptr(), None if norm is None else norm.data_ptr(), self._lambda_init,
+                                   self._eps, 0)
+
+    # read-only
     lambdas = property(lambda self: self._lambdas)
     norm_weight = property(lambda self: self._norm_weight)
     lambda_init = property(lambda self: self._lambda_init)
@@ -461,12 +477,8 @@ class KiviCache:
         for t in tensors:
             t.record_stream(stream)
 
-    def _diff_out(self, weights: DiffWeights, out, shape: tuple, stream, new=torch.empty) -> torch.Tensor:
-        """Checks the weights; the output tensor of a differential attention."""
-        lam, norm = weights._lambdas, weights._norm_weight
-        if (lam.device != self._dev or lam.shape[1] != self.cfg.head_dim or
-                (norm is not None and norm.device != self._dev)):
-            raise ValueError(f"the weights must be on {self._dev} and of head_dim {self.cfg.head_dim}")
+    def _diff_out(self, out, shape: tuple, stream, new=torch.empty) -> torch.Tensor:
+        """The output tensor of a differential attention."""
         if out is None:
             out = new(shape, dtype=torch.float16, device=self._dev)
             if stream is not None:
@@ -481,8 +493,9 @@ class KiviCache:
         q [B, H_q, d] float16 -> out [B, H_q / 2, 2 d] float16."""
         c = self.cfg
         self._on(q, (c.batch, c.h_q, c.head_dim), "q")
-        out = self._diff_out(weights, out, (c.batch, c.h_q // 2, 2 * c.head_dim), stream)
-        self._call("kivi_diff_decode_attn", weights._c, q.data_ptr(), out.data_ptr(), self._stream_here(stream))
+        params = weights._for(self._dev, c.head_dim)
+        out = self._diff_out(out, (c.batch, c.h_q // 2, 2 * c.head_dim), stream)
+        self._call("kivi_diff_decode_attn", params, q.data_ptr(), out.data_ptr(), self._stream_here(stream))
         return out
 
     def append_diff_decode(self, k_new: torch.Tensor, v_new: torch.Tensor, q: torch.Tensor, weights: DiffWeights,
@@ -495,8 +508,9 @@ class KiviCache:
         self._on(k_new, kv, "k_new")
         self._on(v_new, kv, "v_new")
         self._on(q, (c.batch, c.h_q, c.head_dim), "q")
-        out = self._diff_out(weights, out, (c.batch, c.h_q // 2, 2 * c.head_dim), stream)
-        self._call("kivi_append_diff_decode_attn", weights._c, k_new.data_ptr(), v_new.data_ptr(), q.data_ptr(),
+        params = weights._for(self._dev, c.head_dim)
+        out = self._diff_out(out, (c.batch, c.h_q // 2, 2 * c.head_dim), stream)
+        self._call("kivi_append_diff_decode_attn", params, k_new.data_ptr(), v_new.data_ptr(), q.data_ptr(),
                    out.data_ptr(), self._stream_here(stream))
         return out
 
@@ -525,7 +539,8 @@ class KiviCache:
             if len(n_queries) != c.batch:
                 raise ValueError(f"n_queries must have {c.batch} entries")
             counts = (ctypes.c_int64 * c.batch)(*[int(x) for x in n_queries])
-        out = self._diff_out(weights, out, (c.batch, m, c.h_q // 2, 2 * c.head_dim), stream,
+        params = weights._for(self._dev, c.head_dim)
+        out = self._diff_out(out, (c.batch, m, c.h_q // 2, 2 * c.head_dim), stream,
                              torch.empty if counts is None else torch.zeros)
         need = self.diff_prefill_scratch_bytes(m)
         if need == 0:
@@ -536,7 +551,7 @@ class KiviCache:
                 self._made_here((scratch,), stream)
         elif scratch.dtype is not torch.uint8 or scratch.device != self._dev or not scratch.is_contiguous():
             raise ValueError(f"scratch must be a contiguous uint8 tensor on {self._dev}")
-        self._call("kivi_diff_prefill_attn", weights._c, q.data_ptr(), out.data_ptr(), counts, m,
+        self._call("kivi_diff_prefill_attn", params, q.data_ptr(), out.data_ptr(), counts, m,
                    scratch.data_ptr(), scratch.numel(), self._stream_here(stream))
         return out
 
