@@ -472,10 +472,12 @@ int kivi_append_diff_decode_attn(kivi_cache* cache, const kivi_diff_params* para
 
 /* Causal differential attention of a chunk's newest tokens (append the chunk
  * first), as kivi_prefill_attn_ragged.  At 2, 4 and 8 bits and groups of 16, 32
- * or 64, from 64 query rows per kv pair and map on (a sequence's queries x
- * h_q / h_kv), or from 16 where the call is large, keys and values are rounded
- * to fp16 once when they are dequantized; otherwise the products take the codes
- * exactly, as the decode does.
+ * or 64, a sequence with many query rows per kv pair and map (rows = its queries
+ * x h_q / h_kv) has its keys and values rounded to fp16 once when they are
+ * dequantized: from 64 rows on, or from 16 where h_kv / 2 x ceil(rows / 4) x the
+ * tokens that it sees (its own, or its queries and the window) is 2^17 or more.
+ * All others' products take the codes exactly, as the decode does.  This goes
+ * by the sequence's own counts, whatever else is in the call.
  *   q    device fp16 [B][m_max][h_q][d];
  *   out  device fp16 [B][m_max][h_q / 2][2 d];
  *   n_queries  host array of B counts in [0, min(m_max, the sequence's

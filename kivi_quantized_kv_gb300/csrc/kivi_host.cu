@@ -1208,24 +1208,38 @@ cudaError_t diff_all(const kivi_cache& c, const kivi_diff_params& p, const __hal
 int64_t ws_partial_floats(const Geo& g) {
   return static_cast<int64_t>(g.B) * g.hq * g.split_stride * (g.d + 4);
 }
-// Which kernel takes a run of r.n queries a sequence.  The chunk kernel's tile
-// is 128 rows of a kv pair and map, whether they are there or not, the other's
-// four, for which it walks the cache again; but the chunk kernel's start and
-// its second launch cost 12 us more.  4 bits, 32/8 heads of 128, us of the
-// other kernel and of the chunk kernel:
-//   rows              8          16          24          32          64
-//   1 x 4096    21 / 33     22 / 33     24 / 33     29 / 33     40 / 33
-//   4 x 4096    29 / 40     40 / 41     60 / 42     60 / 42
-//   1 x 32768   39 / 58     56 / 58     75 / 59    103 / 59    188 / 59
-//   4 x 32768  105 / 134   189 / 134   355 / 135   355 / 136
-//   16 x 512    23 / 32     45 / 32                 72 / 33
-// So: 64 rows and more, or 16 where the walks of the call's such runs add up.
+// Which kernel takes a sequence of n queries.  The chunk kernel's tile is 128
+// rows of a kv pair and map, whether they are there or not, the other's four,
+// for which it walks the cache again; but the chunk kernel's start and its
+// second launch cost some 12 us.  It also rounds keys and values to fp16 where
+// the other takes the codes exactly, so the choice goes by the sequence's own
+// rows and tokens alone: what a sequence's outputs are rounded to does not
+// depend on the others in the call.  4 bits, 32/8 heads of 128, us of the other
+// kernel and of the chunk kernel, sequences x tokens:
+//   rows              16          24          32          48          64
+//   1 x 2048      19 / 30     21 / 30     23 / 29     25 / 30     29 / 30
+//   1 x 4096      21 / 32     23 / 32     28 / 32     31 / 32     39 / 32
+//   1 x 8192      27 / 35     31 / 35     39 / 35     46 / 35     60 / 35
+//   1 x 32768     55 / 53     74 / 53    102 / 53    130 / 53    187 / 53
+//   4 x 2048      29 / 32     37 / 33     38 / 33     60 / 33     72 / 33
+//   4 x 4096      39 / 40     59 / 40     59 / 40     86 / 40    107 / 41
+//   16 x 512      43 / 32     57 / 32     72 / 32     91 / 33    119 / 33
+//   16 x 2048     72 / 58     98 / 59    125 / 59    172 / 59    228 / 59
+//   16 x 4096    107 / 88    151 / 89    195 / 89    279 / 89    369 / 89
+// (2 bits the same to 2 us, 8 bits up to a tenth more on either side, heads of 64
+// two thirds of both; 32/32 heads as four times the sequences of 32/8.)  So: 64
+// rows and more, or 16 where the sequence's own walks add up to kChunkWork.  A
+// lone sequence then loses up to 8 us at the border (8192 tokens, 16 rows), and
+// batches of shorter sequences with 16 to 63 rows keep the exact kernel where the
+// other would be faster (16 x 2048 with 32 rows: 125 us, not 59): speed that a rule
+// over the whole call had, at the price of outputs that company changed.
 constexpr int64_t kChunkSomeRows = 16, kChunkManyRows = 64;
-constexpr int64_t kChunkWork = int64_t{1} << 17;   // tokens walked by all sequences, kv pairs and passes of four rows
+constexpr int64_t kChunkWork = int64_t{1} << 17;   // tokens walked for a sequence by all kv pairs and passes of four rows
 bool chunk_can(const Geo& g, int64_t nq) { return kivi::chunk_kernel_takes(g) && nq * g.rep >= kChunkSomeRows; }
-int64_t chunk_work(const Geo& g, const Run& r) {
-  const int64_t seen = g.window > 0 ? std::min(r.T, static_cast<int64_t>(g.window) + r.n) : r.T;
-  return r.nb * (g.hkv / 2) * ((r.n * g.rep + 3) / 4) * seen;
+// Tokens walked by the other kernel for one sequence of T tokens and n queries.
+int64_t chunk_work(const Geo& g, int64_t T, int64_t n) {
+  const int64_t seen = g.window > 0 ? std::min(T, static_cast<int64_t>(g.window) + n) : T;
+  return (g.hkv / 2) * ((n * g.rep + 3) / 4) * seen;
 }
 // Tokens of a sequence from which the other kernel is used: its plan counts
 // tokens and positions in 32 bits.
@@ -1389,13 +1403,13 @@ int kivi_diff_prefill_attn(kivi_cache* c, const kivi_diff_params* p, const void*
     cudaStream_t s = static_cast<cudaStream_t>(cuda_stream);
     uint8_t* bytes = static_cast<uint8_t*>(scratch);
     const std::vector<Run> runs = runs_of(*c, count);
-    auto can = [&](const Run& r) { return r.n > 0 && chunk_can(c->g, r.n) && r.T < kChunkMaxTokens; };
-    int64_t work = 0;
-    for (const Run& r : runs)
-      if (can(r)) work += chunk_work(c->g, r);
+    auto by_chunk = [&](const Run& r) {
+      return chunk_can(c->g, r.n) && r.T < kChunkMaxTokens &&
+             (r.n * c->g.rep >= kChunkManyRows || chunk_work(c->g, r.T, r.n) >= kChunkWork);
+    };
     std::vector<Run> few, many;   // by their kernel
     for (const Run& r : runs) {
-      if (r.n > 0) (can(r) && (work >= kChunkWork || r.n * c->g.rep >= kChunkManyRows) ? many : few).push_back(r);
+      if (r.n > 0) (by_chunk(r) ? many : few).push_back(r);
     }
     if (!few.empty()) {
       const int64_t head = diff_head_bytes(c->g, m_max);
