@@ -136,7 +136,7 @@ __global__ void __launch_bounds__(kThreads, kCtas<T, MODE>) rope_qkv_kernel(cons
 
   for (int x = tid; x < nt * 64; x += kThreads) {
     const int t = x >> 6, p = x & 63;
-    float sn = 0.f, cs = 1.f;   // pairs past the last: untouched
+    float sn = 0.f, cs = 1.f;   // pairs past the last (not read)
     if (p < a.pairs) {
       const int64_t pos = a.positions[(static_cast<int64_t>(a.axis[p]) * a.B + bb) * a.n + t0 + t];
       const uint64_t turn = static_cast<uint64_t>(pos) * a.turn[p];
@@ -188,10 +188,17 @@ __global__ void __launch_bounds__(kThreads, kCtas<T, MODE>) rope_qkv_kernel(cons
               float (&z)[8] = j < 2 ? x : y;
               const int o = 4 * (j & 1);
               const float u0 = z[o], v0 = z[o + 1], u1 = z[o + 2], v1 = z[o + 3];
-              z[o] = fmaf(u0, w.x, -v0 * w.y);
-              z[o + 1] = fmaf(u0, w.y, v0 * w.x);
-              z[o + 2] = fmaf(u1, w.z, -v1 * w.w);
-              z[o + 3] = fmaf(u1, w.w, v1 * w.z);
+              // (the thread that holds the last pair also holds channels past
+              // it; turned by nothing, an infinity's neighbour would be NaN)
+              const int p = 8 * item + 2 * j;
+              if (p < a.pairs) {
+                z[o] = fmaf(u0, w.x, -v0 * w.y);
+                z[o + 1] = fmaf(u0, w.y, v0 * w.x);
+              }
+              if (p + 1 < a.pairs) {
+                z[o + 2] = fmaf(u1, w.z, -v1 * w.w);
+                z[o + 3] = fmaf(u1, w.w, v1 * w.z);
+              }
             }
           }
         }
