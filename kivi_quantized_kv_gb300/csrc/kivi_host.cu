@@ -1050,6 +1050,8 @@ PageArgs page_args(const kivi_cache& from, kivi_cache& to) {
   a.dst_unit = to.g.unit_bytes;
   a.sink_v = to.g.sink_v; a.res_k = to.g.res_k; a.res_v = to.g.res_v; a.groups = to.g.groups;
   a.hkv = to.g.hkv; a.d = to.g.d; a.R = to.g.R;
+  a.src_lo = from.g.chk_lo; a.src_hi = from.g.chk_hi; a.src_err = from.g.err;
+  a.dst_lo = to.g.chk_lo; a.dst_hi = to.g.chk_hi; a.dst_err = to.g.err;
   return a;
 }
 }  // namespace

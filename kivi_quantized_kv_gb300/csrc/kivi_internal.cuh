@@ -52,12 +52,16 @@ struct Geo {
 };
 
 // Debug checks (no-ops in the product build).
-__device__ __forceinline__ bool dbg_in_region(const Geo& g, const void* p, int64_t bytes) {
+__device__ __forceinline__ bool dbg_in_range(const uint8_t* lo, const uint8_t* hi, unsigned* err, const void* p,
+                                             int64_t bytes) {
   if constexpr (!kDebugChecks) return true;
   const uint8_t* q = static_cast<const uint8_t*>(p);
-  if (q >= g.chk_lo && bytes >= 0 && q + bytes <= g.chk_hi) return true;
-  atomicOr(g.err, kErrIndex);
+  if (q >= lo && bytes >= 0 && q + bytes <= hi) return true;
+  atomicOr(err, kErrIndex);
   return false;
+}
+__device__ __forceinline__ bool dbg_in_region(const Geo& g, const void* p, int64_t bytes) {
+  return dbg_in_range(g.chk_lo, g.chk_hi, g.err, p, bytes);
 }
 // eight fp16 values: an exponent field of all ones is inf or NaN
 __device__ __forceinline__ void dbg_check_finite(const Geo& g, uint4 v) {
@@ -238,6 +242,9 @@ struct PageArgs {
   int64_t sink_v, res_k, res_v, groups;
   int64_t end;                       // the largest Step::end
   int32_t hkv, d, R, parts;
+  // the checked build: either cache's region and error word
+  const uint8_t *src_lo, *src_hi, *dst_lo, *dst_hi;
+  unsigned *src_err, *dst_err;
   Step step[kMaxSteps];
   int32_t part[kMaxSteps + 1];       // part p: steps [part[p], part[p + 1])
 };

@@ -62,6 +62,7 @@ __global__ void __launch_bounds__(kThreads) pages_kernel(const __grid_constant__
   constexpr int kNext = 16 * kThreads;   // bytes to the thread's next offset
   uint4 now[kCols], kept[CYCLE ? kCols : 1];
   uint32_t on = 0u;   // which of the thread's offsets are live at the step's source
+  uint32_t held = 0u; // (checked build) which of them the kept value has
   for (int i = first; i < last; ++i) {
     const Step& s = a.step[i];
     if (s.src != kStepSame) {
@@ -75,22 +76,29 @@ __global__ void __launch_bounds__(kThreads) pages_kernel(const __grid_constant__
     }
     if (s.src >= 0) {
       const uint8_t* p = a.src + (static_cast<int64_t>(s.src) * a.hkv + h) * a.src_unit + off0;
+      if constexpr (kDebugChecks) {   // what may not be read is not stored either
+        for (int k = 0; k < kCols; ++k)
+          if ((on >> k & 1u) && !dbg_in_range(a.src_lo, a.src_hi, a.src_err, p + k * kNext, 16)) on &= ~(1u << k);
+      }
 #pragma unroll
       for (int k = 0; k < kCols; ++k)
         if (on >> k & 1u) now[k] = *reinterpret_cast<const uint4*>(p + k * kNext);
     } else if (CYCLE && s.src == kStepKept) {
 #pragma unroll
       for (int k = 0; k < kCols; ++k) now[k] = kept[CYCLE ? k : 0];
+      if constexpr (kDebugChecks) on &= held;
     }
     if (CYCLE && s.dst < 0) {
 #pragma unroll
       for (int k = 0; k < kCols; ++k) kept[CYCLE ? k : 0] = now[k];
+      if constexpr (kDebugChecks) held = on;
       continue;
     }
     uint8_t* p = a.dst + (static_cast<int64_t>(s.dst) * a.hkv + h) * a.dst_unit + off0;
 #pragma unroll
     for (int k = 0; k < kCols; ++k)
-      if (on >> k & 1u) *reinterpret_cast<uint4*>(p + k * kNext) = now[k];
+      if ((on >> k & 1u) && dbg_in_range(a.dst_lo, a.dst_hi, a.dst_err, p + k * kNext, 16))
+        *reinterpret_cast<uint4*>(p + k * kNext) = now[k];
   }
 }
 
