@@ -506,7 +506,8 @@ size_t kivi_diff_prefill_scratch_bytes(const kivi_cache* cache, int64_t n_querie
  * affected outputs are not valid.  The checked build of the library
  * (libkivi_debug.so, compiled with KIVI_DEBUG_CHECKS=1) adds two bits that
  * every kernel, appends included, may set: bit 2 = an arena address derived
- * from the plan left the cache region (the access was skipped), bit 3 = an
+ * from the plan left the cache region (the access was skipped, or went to the
+ * cache's first block where a kernel waits for the bytes), bit 3 = an
  * input key, value or query element was inf or NaN (a precondition of the
  * method; the product build does not look).  Unlike every other call this
  * one synchronises `stream` (it returns the value).  Errors: ENULL, ECUDA. */

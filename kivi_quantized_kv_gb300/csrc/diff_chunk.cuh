@@ -285,15 +285,21 @@ static __device__ __noinline__ void tail_rows(const ChunkArgs& a, const Part q, 
   const Tokens tk = tokens_of(a, t, rn, i);
   const int lane = threadIdx.x & 31, head = value ? dw >> 1 : q.m;
   const uint8_t* unit = a.arena + (static_cast<int64_t>(q.b) * g.hkv + 2 * q.j + head) * g.unit_bytes;
-  // row of token x of the tile; null past the last one
+  // row of token x of the tile; null past the last one (checked build: or
+  // outside the cache)
   auto row = [&](int x, bool& sink) -> const uint8_t* {
+    const uint8_t* p;
     sink = x < tk.n0;
-    if (sink) return unit + (value ? g.sink_v : g.sink_k) + static_cast<int64_t>(tk.s0 + x) * D * 4;
-    x -= tk.n0;
-    if (x >= tk.n1) return nullptr;
-    int slot = rn.rs0 + tk.i0 + x;
-    if (slot >= g.R) slot -= g.R;
-    return unit + (value ? g.res_v : g.res_k) + static_cast<int64_t>(slot) * D * 2;
+    if (sink) {
+      p = unit + (value ? g.sink_v : g.sink_k) + static_cast<int64_t>(tk.s0 + x) * D * 4;
+    } else {
+      x -= tk.n0;
+      if (x >= tk.n1) return nullptr;
+      int slot = rn.rs0 + tk.i0 + x;
+      if (slot >= g.R) slot -= g.R;
+      p = unit + (value ? g.res_v : g.res_k) + static_cast<int64_t>(slot) * D * 2;
+    }
+    return dbg_in_region(g, p, sink ? 4 * D : 2 * D) ? p : nullptr;
   };
   // eight channels of a row as fp16
   auto eight = [&](int x, int part) -> uint4 {
@@ -639,12 +645,13 @@ __global__ void __launch_bounds__(kThreads, 1) diff_chunk_kernel(const __grid_co
             uint32_t slot = rn.slot0 + static_cast<uint32_t>(grp + x);
             if (g.window > 0 && slot >= static_cast<uint32_t>(g.n_slots)) slot -= static_cast<uint32_t>(g.n_slots);
             const int64_t at = static_cast<int64_t>(slot) * g.block_bytes;
-            // (debug builds: an address outside the cache reads the first block)
+            // (checked build: where an address is outside the cache, the
+            // cache's first block is read instead, as the barrier counts bytes)
             const bool ok = dbg_in_region(g, k0 + at, g.block_bytes) && dbg_in_region(g, k0 + g.unit_bytes + at, g.block_bytes);
-            const int64_t from = ok ? at : 0;
-            copy_one(dst + x * kb, kk + from, kb, bar);
-            copy_one(dst + ng * kb + x * vb, k0 + from + g.blk_vq, vb, bar);
-            copy_one(dst + ng * (kb + vb) + x * vb, k0 + g.unit_bytes + from + g.blk_vq, vb, bar);
+            const uint8_t* first = a.arena + g.groups;
+            copy_one(dst + x * kb, ok ? kk + at : first, kb, bar);
+            copy_one(dst + ng * kb + x * vb, (ok ? k0 + at : first) + g.blk_vq, vb, bar);
+            copy_one(dst + ng * (kb + vb) + x * vb, (ok ? k0 + g.unit_bytes + at : first) + g.blk_vq, vb, bar);
           }
           grp += ng;
           if (++rs == a.raw_stages) { rs = 0; ph ^= 1u; }

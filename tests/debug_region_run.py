@@ -1,5 +1,6 @@
 """Child-process body of test_gpu_debug_region.py (not a test module): the
-checked build's region check in the copies of sequences.
+checked build's region check in the copies of sequences and in what chunks
+read.
 
 The plans of the library stay inside its caches, so the region that a handle
 believes in is made smaller instead: the end that the check compares with is
@@ -22,6 +23,7 @@ from kivi_quantized_kv_gb300 import build as kbuild  # noqa: E402
 
 kbuild.build(debug_checks=True)
 
+import test_gpu_diff as diff  # noqa: E402
 import test_gpu_pages as pages  # noqa: E402
 from kivi_quantized_kv_gb300 import _abi  # noqa: E402
 
@@ -81,6 +83,17 @@ def main():
     want[1, 1] = before[1, 1]
     res["into_same"] = bool(np.array_equal(pages.units(b), want))
     res["into_flag"], res["into_clean"] = b.read_error(), a.read_error()
+
+    # the chunk kernel: sinks alone, sinks and ring rows, frozen groups as well
+    for name, tokens in (("sinks", 10), ("ring", 70), ("frozen", 400)):
+        cfg = diff.config(h_q=32, h_kv=4, batch=1, sinks=10)
+        f, w = diff.Fed(cfg, [tokens], 3), diff.weights(cfg, 1)
+        q = diff.queries(cfg, 8, 2)   # 64 query rows a kv pair: the chunk kernel's
+        with Shrunk(f.gpu, 1):
+            f.gpu.diff_prefill(q.cuda(), w)
+        res[f"chunk_{name}_flag"] = f.gpu.read_error()
+        diff.close(f.gpu.diff_prefill(q.cuda(), w), *f.expect(q, [8], w))
+        res[f"chunk_{name}_after"] = f.gpu.read_error()
     torch.cuda.synchronize()
     print(json.dumps(res), flush=True)
 

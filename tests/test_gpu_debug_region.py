@@ -1,6 +1,6 @@
-"""The checked build's region check (bit 2) in the copies of sequences:
-an address outside the cache region is reported in
-that cache's word and not accessed, all others are as ever."""
+"""The checked build's region check (bit 2) in the copies of sequences and in
+the chunk kernel: an address outside the cache region is reported in that
+cache's word and not accessed, all others are as ever."""
 import json
 import os
 import subprocess
@@ -34,3 +34,8 @@ def test_reorder(result, what):
 @pytest.mark.parametrize("what", ["from", "into"])
 def test_copy(result, what):
     assert result[f"{what}_flag"] == 4 and result[f"{what}_same"] and result[f"{what}_clean"] == 0, result
+
+
+@pytest.mark.parametrize("what", ["sinks", "ring", "frozen"])
+def test_chunks(result, what):
+    assert result[f"chunk_{what}_flag"] == 4 and result[f"chunk_{what}_after"] == 0, result
