@@ -80,7 +80,10 @@ __device__ __forceinline__ void store8(__half* p, const float (&f)[8]) {
 // MODE 0: pairs (i, i + pairs), pairs a multiple of 8: a thread's two vectors
 //         are the two halves of eight pairs (beyond the pairs: two vectors of
 //         untouched channels).
-// MODE 1: pairs (2i, 2i + 1): a thread's two vectors are eight whole pairs.
+// MODE 1: pairs (2i, 2i + 1), a multiple of 8 of them: a thread's two vectors
+//         are eight whole pairs.
+// MODE 3: the same, any number of pairs (3 x 777 tokens of 24 rows, fp16, which
+//         mode 1 takes too: 6.05 us, 5.75 in mode 1).
 // MODE 2: pairs (i, i + pairs), any number of pairs: sixteen adjacent channels,
 //         whose partners are read one by one.
 // Modes 0 and 2 give the same numbers; mode 2 reads 16 more elements a thread
@@ -110,6 +113,7 @@ __global__ void __launch_bounds__(kThreads, kCtas<T, MODE>) rope_qkv_kernel(cons
     c1 = c0 + 8;
     turned = c0 < 2 * a.pairs;
   }
+  const int left = a.pairs - 8 * item;   // MODE 3: turned pairs from the thread's first on
 
   // rows of this CTA, split over gridDim.z when there are few tokens; the first
   // ones' loads go out before the angles are made
@@ -188,17 +192,22 @@ __global__ void __launch_bounds__(kThreads, kCtas<T, MODE>) rope_qkv_kernel(cons
               float (&z)[8] = j < 2 ? x : y;
               const int o = 4 * (j & 1);
               const float u0 = z[o], v0 = z[o + 1], u1 = z[o + 2], v1 = z[o + 3];
-              // (the thread that holds the last pair also holds channels past
-              // it; turned by nothing, an infinity's neighbour would be NaN)
-              const int p = 8 * item + 2 * j;
-              if (p < a.pairs) {
-                z[o] = fmaf(u0, w.x, -v0 * w.y);
-                z[o + 1] = fmaf(u0, w.y, v0 * w.x);
-              }
-              if (p + 1 < a.pairs) {
-                z[o + 2] = fmaf(u1, w.z, -v1 * w.w);
-                z[o + 3] = fmaf(u1, w.w, v1 * w.z);
-              }
+              z[o] = fmaf(u0, w.x, -v0 * w.y);
+              z[o + 1] = fmaf(u0, w.y, v0 * w.x);
+              z[o + 2] = fmaf(u1, w.z, -v1 * w.w);
+              z[o + 3] = fmaf(u1, w.w, v1 * w.z);
+            }
+          }
+          if (MODE == 3 && left < 8) {
+            // the thread of the last pair also holds channels past it: as they
+            // came (turned by nothing, an infinity's neighbour would be NaN)
+            float x0[8], y0[8];
+            widen<T>(raw[k].a, x0);
+            widen<T>(raw[k].b, y0);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              if (i >= 2 * left) x[i] = x0[i];
+              if (8 + i >= 2 * left) y[i] = y0[i];
             }
           }
         }
@@ -217,14 +226,15 @@ template <class T>
 void launch_mode(const RopeArgs& a, int mode, dim3 grid, cudaStream_t s) {
   if (mode == 0) rope_qkv_kernel<T, 0><<<grid, kThreads, 0, s>>>(a);
   else if (mode == 1) rope_qkv_kernel<T, 1><<<grid, kThreads, 0, s>>>(a);
-  else rope_qkv_kernel<T, 2><<<grid, kThreads, 0, s>>>(a);
+  else if (mode == 2) rope_qkv_kernel<T, 2><<<grid, kThreads, 0, s>>>(a);
+  else rope_qkv_kernel<T, 3><<<grid, kThreads, 0, s>>>(a);
 }
 
 }  // namespace
 
 cudaError_t launch_rope_qkv(RopeArgs a, int dtype, bool adjacent, int num_sms, const int64_t* n_tokens,
                             cudaStream_t s) {
-  const int mode = adjacent ? 1 : a.pairs % 8 == 0 ? 0 : 2;
+  const int mode = adjacent ? (a.pairs % 8 == 0 ? 1 : 3) : a.pairs % 8 == 0 ? 0 : 2;
   const int slots = kThreads / (a.d / 16), heads = a.hq + 2 * a.hk;
   // Four tokens a CTA share its start (2400 tokens of 48 rows in bf16 11.4 us,
   // 14.1 with one; 20000 79 and 107); one where four would leave SMs with little
