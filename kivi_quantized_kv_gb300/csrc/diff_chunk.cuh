@@ -285,26 +285,23 @@ static __device__ __noinline__ void tail_rows(const ChunkArgs& a, const Part q, 
   const Tokens tk = tokens_of(a, t, rn, i);
   const int lane = threadIdx.x & 31, head = value ? dw >> 1 : q.m;
   const uint8_t* unit = a.arena + (static_cast<int64_t>(q.b) * g.hkv + 2 * q.j + head) * g.unit_bytes;
-  // row of token x of the tile; null past the last one (checked build: or
-  // outside the cache)
+  // row of token x of the tile; null past the last one
   auto row = [&](int x, bool& sink) -> const uint8_t* {
-    const uint8_t* p;
     sink = x < tk.n0;
-    if (sink) {
-      p = unit + (value ? g.sink_v : g.sink_k) + static_cast<int64_t>(tk.s0 + x) * D * 4;
-    } else {
-      x -= tk.n0;
-      if (x >= tk.n1) return nullptr;
-      int slot = rn.rs0 + tk.i0 + x;
-      if (slot >= g.R) slot -= g.R;
-      p = unit + (value ? g.res_v : g.res_k) + static_cast<int64_t>(slot) * D * 2;
-    }
-    return dbg_in_region(g, p, sink ? 4 * D : 2 * D) ? p : nullptr;
+    if (sink) return unit + (value ? g.sink_v : g.sink_k) + static_cast<int64_t>(tk.s0 + x) * D * 4;
+    x -= tk.n0;
+    if (x >= tk.n1) return nullptr;
+    int slot = rn.rs0 + tk.i0 + x;
+    if (slot >= g.R) slot -= g.R;
+    return unit + (value ? g.res_v : g.res_k) + static_cast<int64_t>(slot) * D * 2;
   };
   // eight channels of a row as fp16
   auto eight = [&](int x, int part) -> uint4 {
     bool sink;
     const uint8_t* p = row(x, sink);
+    if constexpr (kDebugChecks) {   // a row outside the cache reads as zeros
+      if (p && !dbg_in_region(g, p, sink ? 4 * D : 2 * D)) p = nullptr;
+    }
     uint4 v = make_uint4(0u, 0u, 0u, 0u);
     if (p && sink) {
       const float4 f = reinterpret_cast<const float4*>(p)[2 * part], h = reinterpret_cast<const float4*>(p)[2 * part + 1];
