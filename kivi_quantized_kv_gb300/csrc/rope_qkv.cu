@@ -82,13 +82,16 @@ __device__ __forceinline__ void store8(__half* p, const float (&f)[8]) {
 //         untouched channels).
 // MODE 1: pairs (2i, 2i + 1), a multiple of 8 of them: a thread's two vectors
 //         are eight whole pairs.
-// MODE 3: the same, any number of pairs (3 x 777 tokens of 24 rows, fp16, which
-//         mode 1 takes too: 6.05 us, 5.75 in mode 1).
 // MODE 2: pairs (i, i + pairs), any number of pairs: sixteen adjacent channels,
 //         whose partners are read one by one.
-// Modes 0 and 2 give the same numbers; mode 2 reads 16 more elements a thread
-// (20000 tokens in bf16: 227 us, where mode 0 takes 79), so it takes only the
-// sections that mode 0 cannot.
+// MODE 3: pairs (2i, 2i + 1), any number of pairs: as mode 1, but the thread of
+//         the last pair leaves the channels past it as they came (turned by
+//         nothing, an infinity's neighbour would be NaN).
+// Modes 0 and 2 give the same numbers, and so do 1 and 3 where both can.  Mode 2
+// reads 16 more elements a thread (20000 tokens in bf16: 227 us, where mode 0
+// takes 79), mode 3 tests each pair (3 x 777 tokens of 24 rows in fp16: 6.0 us,
+// 5.8 in mode 1; 20000 in bf16 79 in both), so they take only the sections that
+// the others cannot.
 template <class T, int MODE>
 __global__ void __launch_bounds__(kThreads, kCtas<T, MODE>) rope_qkv_kernel(const __grid_constant__ RopeArgs a) {
   __shared__ float4 tab[kRopeTokens][4][8];   // token, pair (2 j, 2 j + 1) of an item, item: (cos, sin) twice
@@ -192,22 +195,14 @@ __global__ void __launch_bounds__(kThreads, kCtas<T, MODE>) rope_qkv_kernel(cons
               float (&z)[8] = j < 2 ? x : y;
               const int o = 4 * (j & 1);
               const float u0 = z[o], v0 = z[o + 1], u1 = z[o + 2], v1 = z[o + 3];
-              z[o] = fmaf(u0, w.x, -v0 * w.y);
-              z[o + 1] = fmaf(u0, w.y, v0 * w.x);
-              z[o + 2] = fmaf(u1, w.z, -v1 * w.w);
-              z[o + 3] = fmaf(u1, w.w, v1 * w.z);
-            }
-          }
-          if (MODE == 3 && left < 8) {
-            // the thread of the last pair also holds channels past it: as they
-            // came (turned by nothing, an infinity's neighbour would be NaN)
-            float x0[8], y0[8];
-            widen<T>(raw[k].a, x0);
-            widen<T>(raw[k].b, y0);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              if (i >= 2 * left) x[i] = x0[i];
-              if (8 + i >= 2 * left) y[i] = y0[i];
+              if (MODE == 1 || 2 * j < left) {
+                z[o] = fmaf(u0, w.x, -v0 * w.y);
+                z[o + 1] = fmaf(u0, w.y, v0 * w.x);
+              }
+              if (MODE == 1 || 2 * j + 1 < left) {
+                z[o + 2] = fmaf(u1, w.z, -v1 * w.w);
+                z[o + 3] = fmaf(u1, w.w, v1 * w.z);
+              }
             }
           }
         }
