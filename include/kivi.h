@@ -388,6 +388,7 @@ typedef struct kivi_qkv {
 /* Turns the query and key rows by their tokens' positions and lays all three
  * out for this cache: what kivi_append, kivi_append_decode_attn and the
  * attention calls take, in one launch.
+ *   n_max      1 to 2^31.
  *   positions  device int64 [n_axes][B][n_max]; any sign.  The angle is off
  *              by at most |position| * 2^-52 turns plus 2^-24 of a half turn.
  *   n_tokens   host array of B counts in [0, n_max], or NULL (n_max each).
@@ -411,15 +412,17 @@ int kivi_rope_qkv(const kivi_cache* cache, const kivi_rope_params* rope, const k
  * keeps it, -1 frees it: its token count becomes 0).  Forks (an entry
  * several times), chains and cycles are all allowed.  Only live bytes move
  * (sinks, ring tokens not yet frozen, frozen blocks), each once; bytes of a
- * unit that hold nothing for the new token count stay as they were.  One
- * launch for up to 96 moved sequences.  In a captured graph the copies of
+ * unit that hold nothing for the new token count stay as they were.  A launch
+ * holds 96 steps, one for each moved sequence and one more for each cycle (so
+ * 96 sequences at most, 64 where all are swaps); longer maps take more launches.
+ * In a captured graph the copies of
  * the map and of the token counts at capture are replayed.
  * Errors: ENULL (also: no host memory), EINVAL, ECUDA (the token counts are
  * then as before, the moved sequences' bytes undefined). */
 int kivi_cache_reorder(kivi_cache* cache, const int32_t* src, void* cuda_stream);
 
 /* Copies sequences of `src` into `dst`: sequence dst_seq[i] of dst becomes
- * sequence src_seq[i] of src, i < n (host arrays; dst_seq without
+ * sequence src_seq[i] of src, i < n, n >= 1 (host arrays; dst_seq without
  * repetition, src_seq may repeat).  The caches are different handles over
  * arenas that do not overlap, on the same device, with equal parameters but
  * for h_q, batch and max_tokens.  Live bytes only, as kivi_cache_reorder.
@@ -437,7 +440,9 @@ int kivi_cache_copy(kivi_cache* dst, const kivi_cache* src, const int32_t* dst_s
  * map's keys K1 and channels 0..d-1 of the value V, kv head 2j + 1 the second
  * map's keys K2 and channels d..2d-1.  Differential head i (i < h_q / 2)
  * reads kv pair i / (h_q / h_kv); its query rows are query heads 2i (q1) and
- * 2i + 1 (q2).  Over the tokens that the cache's plain attention would see,
+ * 2i + 1 (q2).  (A model that keeps all first maps before all second ones permutes
+ * the rows of its q and k projections once: new head 2i + m = old head i + m h / 2.
+ * Its value heads of 2 d channels lie as they should.)  Over the tokens that the cache's plain attention would see,
  *   o = softmax(q1 K1' / sqrt(d)) V - lambda softmax(q2 K2' / sqrt(d)) V,
  *   lambda = exp(lq1 . lk1) - exp(lq2 . lk2) + lambda_init,
  * and with a norm
@@ -499,9 +504,10 @@ size_t kivi_diff_prefill_scratch_bytes(const kivi_cache* cache, int64_t n_querie
 /* Reads and clears the device error word that the cache's attention launches
  * (kivi_decode_attn, kivi_append_decode_attn, kivi_prefill_attn,
  * kivi_decode_attn_noalloc and the differential ones, with their variants) set instead of hanging:
- * bit 0 = a bulk copy into shared memory (or, in kivi_diff_prefill_attn, a step
- * of the kernel's pipeline) did not complete within its bounded wait (2 s, or
- * the limit of kivi_debug_set_wait_limit), bit 1 = a warp
+ * bit 0 = a bulk copy into shared memory did not complete within its bounded
+ * wait (2 s, or the limit of kivi_debug_set_wait_limit) or, in
+ * kivi_diff_prefill_attn, a step of the kernel's pipeline within its own (2 s
+ * whatever the limit, which only the copying warp's waits follow), bit 1 = a warp
  * waited in vain for its combine slot to be released.  Either bit means the
  * affected outputs are not valid.  The checked build of the library
  * (libkivi_debug.so, compiled with KIVI_DEBUG_CHECKS=1) adds two bits that

@@ -5,10 +5,16 @@
 // Measured (heads of 128): 8 x 4096 tokens, 32/32 heads, 4 bits 55 us (3.0 TB/s
 // of cache bytes; the plain decode of the same cache, half the products, 47);
 // 4 x 32768, 32/8 heads, 2 bits 51 us (1.8 TB/s); 32 windows of 4096, 8 bits, groups
-// of 64, 73 us (3.7 TB/s); one sequence of 256 tokens 9 us.  Bound by instruction
-// issue: 28 M warp instructions for the first (860 per warp and group of 32
-// tokens), issue slots 52 % busy with the sixteen warps that 128 registers
-// allow, tensor pipe 27 %, DRAM reads as many as the cache's bytes.
+// of 64, 73 us (3.7 TB/s); one sequence of 256 tokens 9 us.  The first case at
+// 1 to 8 bits: 67, 54, 69, 55, 79, 84, 80 and 60 us (bit streams read and shift
+// more words a code).  The fused step takes 1 us more than the decode, a freezing
+// step among 32 included.
+// Bound by a group's instructions and their latencies: 28 M warp instructions
+// for the first case (860 per warp and group of 32 tokens, some 240 of them for
+// the codes), issue slots 52 % busy (35 % for the windows, ten warps an SM) with
+// the sixteen warps that 128 registers allow, whose first stalls are fixed
+// latencies (1.9 warps an issue), the math pipe and shared memory (1.0 each);
+// tensor pipe 27 %, DRAM reads as many as the cache's bytes.
 #include "diff_launch.cuh"
 
 namespace kivi {

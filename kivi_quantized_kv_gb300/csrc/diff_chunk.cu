@@ -3,8 +3,8 @@
 // there); diff_chunk_b*.cu instantiate the first per code width.
 //
 // Measured (heads of 128): 512 queries of 32/8 heads over 2 x 8192 tokens of 4 bits
-// 268 us, 0.74 PFLOP/s (0.38 of the library's bf16 product): the first kernel
-// 246, the merge 20.  Tensor pipe 35 %, issue slots 58 % of the 18 warps that 96
+// 271 us, 0.74 PFLOP/s (0.38 of the library's bf16 product): the first kernel
+// 246, the merge 20; of 2 bits 273, of 8 bits 264; heads of 64 196.  Tensor pipe 35 %, issue slots 58 % of the 18 warps that 96
 // registers allow.  Bound by the dequantizing groups, a CTA's busiest role (some
 // 1800 warp instructions and 48 KB of shared-memory stores for a token tile of
 // 2250 cycles, of which the products take 770): a third group of them, at 80
@@ -15,7 +15,9 @@ namespace kivi {
 
 // Word-rule widths (their codes unpack two at a time into fp16 with one
 // AND-OR) and groups that divide a token tile, whose packed rows are whole
-// (bulk copies).  The other caches keep the kernel of diff_mma.cuh.
+// (bulk copies).  The other caches keep the kernel of diff_mma.cuh, which walks the
+// cache once for four query rows: 3.0 ms at 3 bits, 2.8 at 4 and 3.8 at 8 with
+// groups of 128.
 bool chunk_kernel_takes(const Geo& g) { return word_rule(g.bits) && kChunkTokens % g.G == 0; }
 
 template <int D, int AHEAD>

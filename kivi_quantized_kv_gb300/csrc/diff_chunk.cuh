@@ -399,9 +399,11 @@ __global__ void __launch_bounds__(kThreads, 1) diff_chunk_kernel(const __grid_co
   fence_after();
   const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(tmem_slot);
 
-  // Every wait is bounded.  A warp whose wait ran out waits no more, issues and
-  // copies nothing more, and goes on through the barriers; the others' waits for
-  // it run out in turn, and the launch ends with the error bit set.
+  // Every wait is bounded: the copying warp's by a.wait_ns, the others', whose
+  // lanes give up one by one, by kWaitNs, which no test makes shorter.  A warp
+  // whose wait ran out waits no more, issues and copies nothing more, and goes on
+  // through the barriers; the others' waits for it run out in turn, and the launch
+  // ends with the error bit set.
   bool gone = false;
   auto wait = [&](uint32_t bar, uint32_t parity) {
     if (gone || mbar_wait(bar, parity, kWaitNs)) return;

@@ -38,12 +38,13 @@
 // eight pairs, which take the positions of a range in turn.  At a unit's end the
 // pairs' states meet in a tree over shared memory; a unit inside one CTA is
 // finished there, else the CTA writes a partial record (a CTA shares at most
-// its first and its last unit, so two records a CTA), and the last CTA to
-// sign in merges: the difference and the norm need both maps and all 2 d
+// its first and its last unit, so two records a CTA, or one where the launch
+// gives each unit whole CTAs), and the last CTA to sign in merges: the difference and the norm need both maps and all 2 d
 // channels, so they come last, once.
 //
-// Bound by: instruction issue, as the decode (each code is unpacked once for
-// all query rows and both maps); the figures are beside the launch in diff.cu.
+// Bound by: the instructions of a group and their latencies at sixteen warps an
+// SM (each code is unpacked once for all query rows and both maps; issue slots
+// are half busy); the figures are beside the launch in diff.cu.
 #pragma once
 
 #include "decode_mma.cuh"

@@ -334,7 +334,7 @@ struct ChunkArgs {
   __half* out;            // [B][q_rows][h_q / 2][2 d]
   float* records;         // [units + CTAs][2 d + 4][128]: o by channel, then m, l of even and of odd tiles
   unsigned* error;
-  unsigned long long wait_ns;   // how long a warp waits before it gives up
+  unsigned long long wait_ns;   // how long the copying warp waits before it gives up (the other roles 2 s)
   const float* lambdas;
   const float* weight;
   float lambda_init, eps;

@@ -25,8 +25,9 @@
 //
 // Measured, read and written bytes: four sequences of up to 32768 tokens of 8
 // bits into another cache (420 MB) 62 us, 6.8 TB/s (a plain copy's rate); two
-// sequences of 4096 tokens forked to six others (168 MB) 27 us, 6.2 TB/s; one of
-// 256 tokens 2 us, a launch's own time.
+// sequences of 4096 tokens forked to six others (168 MB) 27 us, 6.2 TB/s, eight of
+// them turned round a cycle (336 MB) 54 us and swapped in pairs 52 us; one of 256
+// tokens 2 us, a launch's own time.
 #include "kivi_internal.cuh"
 
 namespace kivi {
