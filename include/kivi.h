@@ -450,12 +450,13 @@ int kivi_cache_copy(kivi_cache* dst, const kivi_cache* src, const int32_t* dst_s
  * over a head's 2 d channels.  A row that sees no token (a sequence without
  * tokens, or a query whose window the cache no longer holds) gives zeros, also
  * with norm_eps 0. */
+#define KIVI_DIFF_EXACT_CODES 1   /* kivi_diff_prefill_attn rounds no keys and values, whatever the rows */
 typedef struct kivi_diff_params {
   const float* lambdas;       /* device fp32 [4][d]: lq1, lk1, lq2, lk2; read by the launch */
   const float* norm_weight;   /* device fp32 [2 d], 8-byte aligned, or NULL: no norm (and no 1 - lambda_init) */
   float lambda_init;
   float norm_eps;             /* >= 0 */
-  int64_t reserved;           /* 0 */
+  int64_t flags;              /* 0 or KIVI_DIFF_EXACT_CODES */
 } kivi_diff_params;
 
 /* Differential decode attention.
@@ -482,7 +483,10 @@ int kivi_append_diff_decode_attn(kivi_cache* cache, const kivi_diff_params* para
  * dequantized: from 64 rows on, or from 16 where h_kv / 2 x ceil(rows / 4) x the
  * tokens that it sees (its own, or its queries and the window) is 2^17 or more.
  * All others' products take the codes exactly, as the decode does.  This goes
- * by the sequence's own counts, whatever else is in the call.
+ * by the sequence's own counts, whatever else is in the call.  The rounding
+ * leaves outputs off by some 1e-3 of their 2-norm where exact codes leave fp16's own
+ * 2e-4; with KIVI_DIFF_EXACT_CODES no sequence's are rounded, and chunks of many
+ * rows take up to ten times as long.
  *   q    device fp16 [B][m_max][h_q][d];
  *   out  device fp16 [B][m_max][h_q / 2][2 d];
  *   n_queries  host array of B counts in [0, min(m_max, the sequence's

@@ -32,6 +32,7 @@ KIVI_F16, KIVI_BF16, KIVI_F32 = range(3)
 KIVI_ROPE_AXES = 4
 KIVI_ROPE_BLOCKS, KIVI_ROPE_INTERLEAVED = range(2)
 KIVI_ROPE_HALVES, KIVI_ROPE_ADJACENT = range(2)
+KIVI_DIFF_EXACT_CODES = 1
 
 
 class KiviParams(ctypes.Structure):
@@ -67,7 +68,7 @@ class KiviQkv(ctypes.Structure):
 
 class KiviDiffParams(ctypes.Structure):
     _fields_ = [("lambdas", ctypes.c_void_p), ("norm_weight", ctypes.c_void_p), ("lambda_init", ctypes.c_float),
-                ("norm_eps", ctypes.c_float), ("reserved", ctypes.c_int64)]
+                ("norm_eps", ctypes.c_float), ("flags", ctypes.c_int64)]
 
 
 class KiviError(RuntimeError):

@@ -101,7 +101,7 @@ class DiffWeights:
         if norm_weight is not None and tuple(norm_weight.shape) != (2 * lambdas.shape[1],):
             raise ValueError(f"norm_weight must have shape {(2 * lambdas.shape[1],)}, got {tuple(norm_weight.shape)}")
 
-    def _for(self, device: torch.device, d: int) -> _abi.KiviDiffParams:
+    def _for(self, device: torch.device, d: int, flags: int = 0) -> _abi.KiviDiffParams:
         """What a launch of a cache on `device` with this head_dim takes.  The
         tensors are looked at in each call: their storage may have been exchanged."""
         lam, norm = self._lambdas, self._norm_weight
@@ -112,7 +112,7 @@ class DiffWeights:
             self._check()
             raise ValueError(f"the weights must be on {device} and of head_dim {d}")
         return _abi.KiviDiffParams(lam.data_ptr(), None if norm is None else norm.data_ptr(), self._lambda_init,
-                                   self._eps, 0)
+                                   self._eps, flags)
 
     # read-only
     lambdas = property(lambda self: self._lambdas)
@@ -515,22 +515,24 @@ class KiviCache:
         return out
 
     def diff_prefill(self, q: torch.Tensor, weights: DiffWeights, out: torch.Tensor | None = None,
-                     scratch: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+                     scratch: torch.Tensor | None = None, stream=None, exact: bool = False) -> torch.Tensor:
         """Causal differential attention of the M newest tokens (append the
         chunk first): q [B, M, H_q, d] float16 -> out [B, M, H_q / 2, 2 d]
         float16 (kivi_diff_prefill_attn).  scratch: a uint8 device tensor of
         diff_prefill_scratch_bytes(M) bytes; by default each call takes one
-        of its own, so captured graphs and streams share none."""
-        return self._diff_prefill(q, None, weights, out, scratch, stream)
+        of its own, so captured graphs and streams share none.  exact: keys
+        and values of large chunks are not rounded to fp16 either, at up to ten
+        times the time (KIVI_DIFF_EXACT_CODES)."""
+        return self._diff_prefill(q, None, weights, out, scratch, stream, exact)
 
     def diff_prefill_ragged(self, q: torch.Tensor, n_queries, weights: DiffWeights, out: torch.Tensor | None = None,
-                            scratch: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+                            scratch: torch.Tensor | None = None, stream=None, exact: bool = False) -> torch.Tensor:
         """diff_prefill of sequence b's n_queries[b] newest tokens; rows past a
         sequence's count are left as they are in `out` (zeros when out is
         None)."""
-        return self._diff_prefill(q, n_queries, weights, out, scratch, stream)
+        return self._diff_prefill(q, n_queries, weights, out, scratch, stream, exact)
 
-    def _diff_prefill(self, q, n_queries, weights, out, scratch, stream):
+    def _diff_prefill(self, q, n_queries, weights, out, scratch, stream, exact):
         c = self.cfg
         m = q.shape[1] if q.dim() == 4 else -1
         self._on(q, (c.batch, m, c.h_q, c.head_dim), "q")
@@ -539,7 +541,7 @@ class KiviCache:
             if len(n_queries) != c.batch:
                 raise ValueError(f"n_queries must have {c.batch} entries")
             counts = (ctypes.c_int64 * c.batch)(*[int(x) for x in n_queries])
-        params = weights._for(self._dev, c.head_dim)
+        params = weights._for(self._dev, c.head_dim, _abi.KIVI_DIFF_EXACT_CODES if exact else 0)
         out = self._diff_out(out, (c.batch, m, c.h_q // 2, 2 * c.head_dim), stream,
                              torch.empty if counts is None else torch.zeros)
         need = self.diff_prefill_scratch_bytes(m)

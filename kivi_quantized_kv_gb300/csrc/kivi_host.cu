@@ -1122,7 +1122,7 @@ int diff_params_ok(const kivi_cache& c, const kivi_diff_params* p) {
   const Geo& g = c.g;
   // pairs of kv heads and of query heads; no outlier tables, keys as they arrive
   if (g.hkv % 2 != 0 || g.n_out != 0 || g.rope_l2b != 0.0) return KIVI_EINVAL;
-  if (p->reserved != 0 || !std::isfinite(p->lambda_init) || !std::isfinite(p->norm_eps) || p->norm_eps < 0.f)
+  if ((p->flags & ~int64_t{KIVI_DIFF_EXACT_CODES}) != 0 || !std::isfinite(p->lambda_init) || !std::isfinite(p->norm_eps) || p->norm_eps < 0.f)
     return KIVI_EINVAL;
   if (!aligned(p->lambdas, 4) || !aligned(p->norm_weight, 8)) return KIVI_EALIGN;
   return KIVI_OK;
@@ -1406,7 +1406,7 @@ int kivi_diff_prefill_attn(kivi_cache* c, const kivi_diff_params* p, const void*
     uint8_t* bytes = static_cast<uint8_t*>(scratch);
     const std::vector<Run> runs = runs_of(*c, count);
     auto by_chunk = [&](const Run& r) {
-      return chunk_can(c->g, r.n) && r.T < kChunkMaxTokens &&
+      return (p->flags & KIVI_DIFF_EXACT_CODES) == 0 && chunk_can(c->g, r.n) && r.T < kChunkMaxTokens &&
              (r.n * c->g.rep >= kChunkManyRows || chunk_work(c->g, r.T, r.n) >= kChunkWork);
     };
     std::vector<Run> few, many;   // by their kernel
